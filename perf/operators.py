@@ -48,33 +48,33 @@ def listed():
          "Hkv": 4, "d": 64, "dtype": "fp16", "rot": 64, "interleaved": True},
         # a long prompt written into an empty paged cache and read back
         {"name": "cache prompt 4x8192 e4m3", "op": "cache", "B": 4, "lo": 0, "hi": 0, "new_lo": 8192,
-         "new_hi": 8192, "Hkv": 8, "d": 128, "dtype": "bf16", "heads_first": True, "fmt": "e4m3", "page": 256},
+         "new_hi": 8192, "Hkv": 8, "d": 128, "dtype": "bf16", "fmt": "e4m3", "page": 256},
         # ragged prompts behind ragged prefixes, small pages
         {"name": "cache ragged 16 int8", "op": "cache", "B": 16, "lo": 3, "hi": 700, "new_lo": 256,
-         "new_hi": 8192, "Hkv": 8, "d": 64, "dtype": "fp16", "heads_first": False, "fmt": "int8", "page": 64},
+         "new_hi": 8192, "Hkv": 8, "d": 64, "dtype": "fp16", "fmt": "int8", "page": 64},
         # single new tokens behind short prefixes: latency
         {"name": "cache decode 64x1 int8", "op": "cache", "B": 64, "lo": 16, "hi": 200, "new_lo": 1,
-         "new_hi": 1, "Hkv": 8, "d": 128, "dtype": "bf16", "heads_first": True, "fmt": "int8", "page": 64},
+         "new_hi": 1, "Hkv": 8, "d": 128, "dtype": "bf16", "fmt": "int8", "page": 64},
         # a full serving batch: single tokens against long ragged paged caches
         {"name": "attend 64x1 to 32768 e4m3", "op": "attend", "B": 64, "Sq": 1, "lo": 1024,
-         "hi": 32768, "H": 32, "Hkv": 8, "d": 128, "dtype": "bf16", "heads_first": True, "fmt": "e4m3", "page": 256,
+         "hi": 32768, "H": 32, "Hkv": 8, "d": 128, "dtype": "bf16", "fmt": "e4m3", "page": 256,
          "causal": False, "window": -1, "softcap": 0.0, "alibi": False},
         # one long sequence, a contiguous cache, no shared heads: the split over the keys
         {"name": "attend 1x1 to 32749 int8", "op": "attend", "B": 1, "Sq": 1, "lo": 32749,
-         "hi": 32749, "H": 16, "Hkv": 16, "d": 64, "dtype": "fp16", "heads_first": True, "fmt": "int8", "page": 0,
+         "hi": 32749, "H": 16, "Hkv": 16, "d": 64, "dtype": "fp16", "fmt": "int8", "page": 0,
          "causal": False, "window": -1, "softcap": 0.0, "alibi": False},
         # three drafted tokens per sequence, every mask and score term
         {"name": "attend 13x3 masked int8", "op": "attend", "B": 13, "Sq": 3, "lo": 100, "hi": 9000,
-         "H": 16, "Hkv": 4, "d": 128, "dtype": "bf16", "heads_first": False, "fmt": "int8", "page": 64, "causal": True,
+         "H": 16, "Hkv": 4, "d": 128, "dtype": "bf16", "fmt": "int8", "page": 64, "causal": True,
          "window": 4096, "softcap": 30.0, "alibi": True},
         # the input side of a decoding step
         {"name": "step 64x1 e4m3", "op": "step", "B": 64, "lo": 1024, "hi": 32768, "new_lo": 1,
          "new_hi": 1, "H": 32, "Hkv": 8, "d": 128, "dtype": "bf16", "rot": 128,
-         "interleaved": False, "heads_first": True, "fmt": "e4m3", "page": 256},
+         "interleaved": False, "fmt": "e4m3", "page": 256},
         # the input side of a chunked prefill, ragged chunks
         {"name": "step chunks 4x2048 int8", "op": "step", "B": 4, "lo": 4000, "hi": 6144,
          "new_lo": 1500, "new_hi": 2048, "H": 32, "Hkv": 8, "d": 64, "dtype": "fp16", "rot": 64,
-         "interleaved": False, "heads_first": True, "fmt": "int8", "page": 64},
+         "interleaved": False, "fmt": "int8", "page": 64},
     ]
 
 
@@ -95,7 +95,6 @@ def draw(rng):
     if op in ("cache", "attend", "step"):
         c["fmt"] = rng.choice(["e4m3", "int8"])
         c["page"] = rng.choice([0, 64, 128, 256])
-        c["heads_first"] = rng.random() < 0.7
     if op in ("norm_rope", "norm_rope_grad"):
         c["S"] = _log(rng, 1, 8192)
         c["B"] = max(1, min(_log(rng, 1, 64), 12000 // c["S"]))
@@ -172,8 +171,6 @@ def _cache(case, lens, capacity, g, seed):
         rows = int(capacity.max())
         shape, scales = (B, rows, Hkv, d), (B, Hkv, rows)
     top = TOP[case["fmt"]]
-    if case["heads_first"]:
-        shape = (shape[0], Hkv, shape[1], d)
     for name in ("k", "v"):
         codes = torch.empty(shape, dtype=torch.float8_e4m3fn if case["fmt"] == "e4m3" else torch.int8, device="cuda")
         flat = codes.view(-1, d)
@@ -181,7 +178,7 @@ def _cache(case, lens, capacity, g, seed):
             x = torch.randn((min(1 << 19, flat.shape[0] - i), d), generator=g, device="cuda")
             x = x * (top / x.abs().amax(1, keepdim=True))
             flat[i:i + (1 << 19)] = x.to(codes.dtype) if case["fmt"] == "e4m3" else x.round().to(torch.int8)
-        s[name + "_cache"] = codes.transpose(1, 2) if case["heads_first"] else codes
+        s[name + "_cache"] = codes
         s[name + "_scale"] = torch.exp(0.3 * torch.randn(scales, generator=g, device="cuda")) * (3.0 / top)
     s["lens"] = lens.int().cuda()
     return s
