@@ -579,7 +579,9 @@ __global__ void __launch_bounds__(kBwdThreads, kRowsBwdBlocksPerSm)
       float2 v[8];
       read_row(slot + kGroupBytes + at0, next, w);
       unpack16<BF16>(w, v);
-      const float r = inv_rms<D>(v, p.eps);
+      // (heads behind the last are zeros here: with eps 0 their r would be infinite, and what they add
+      // to dw a NaN)
+      const float rms = inv_rms<D>(v, p.eps), r = store ? rms : 0.f;
       float2 dot = both(0.f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
