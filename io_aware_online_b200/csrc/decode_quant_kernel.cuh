@@ -470,6 +470,9 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
   }
+  // every lane waits on both barriers and, where the scales come word by word, arrives on the first:
+  // shuffles alone would not order that behind their initialisation
+  __syncwarp();
 
   // ---- this warp's share of the line of tiles.  (The host has made sure that 31 bits count it.)
   const int pairs = p.Hkv * p.groups;  // pairs of one sequence

@@ -1,0 +1,123 @@
+"""Forms of the attention over the 8-bit cache that the other checks leave out, against plain
+attention in 64 bits on the values that the codes stand for (on the GPU).
+
+Bounds, as in the other checks of this operator: with A the largest sum of a score's magnitudes,
+ds = 2^-17 (1 + 2^-4) A + softcap 2^-20 + 2^-21 slope distance for the scores;
+  LSE: ds + 2^-20 (1 + |LSE|)
+  O:   (pr + 2 ds + 2^-18) sum_j w_j |v_j| + u |O| + half a subnormal step, pr the rounding of the
+       probabilities (2^-11, for fp16 outputs in two parts 2^-21), u that of the output."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FMT = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from io_aware_online_b200 import build
+    build.build()
+    import io_aware_online_b200 as fa
+    fa.load()
+    fa.fa_device_status(clear=True)
+    yield
+    assert fa.fa_device_status(clear=True) == 0
+
+
+def fa():
+    import io_aware_online_b200 as m
+    return m
+
+
+def codes(shape, fmt, seed):
+    """Random codes over the whole format (an E4M3 NaN left out)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    c = torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)
+    if fmt == "e4m3":
+        c = torch.where((c & 0x7f) == 0x7f, c & 0xf7, c)
+        return c.view(FMT[fmt])
+    return c.view(torch.int8)
+
+
+def scales(shape, top, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.exp(0.5 * torch.randn(shape, generator=g, device=DEV)) * (2.0 / top)
+
+
+def contiguous_cache(B, n, Hkv, d, fmt, heads_first=False, seed=0):
+    """k, v codes [B, n, Hkv, d] and scales [B, Hkv, n] of a contiguous cache."""
+    shape = (B, Hkv, n, d) if heads_first else (B, n, Hkv, d)
+    kv = [codes(shape, fmt, seed + i) for i in range(2)]
+    kv = [t.transpose(1, 2) for t in kv] if heads_first else kv
+    top = 448.0 if fmt == "e4m3" else 127.0
+    return (*kv, *(scales((B, Hkv, n), top, seed + 2 + i) for i in range(2)))
+
+
+def values(c):
+    """fp64 keys and values [B, n, Hkv, d] of a contiguous cache."""
+    k, v, ks, vs = c
+    return [t.double() * s.double().transpose(1, 2)[..., None] for t, s in ((k, ks), (v, vs))]
+
+
+def check(out, lse, q, k, v, lens, causal=False, window=(-1, -1), softcap=0.0, slopes=None):
+    """Every sequence by itself, every query row and head."""
+    B, Sq, H, d = q.shape
+    G = H // k.shape[2]
+    u = torch.finfo(q.dtype).eps / 2
+    pr = 2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -21
+    for b, n in enumerate(lens):
+        kb, vb = (t[b, :n].repeat_interleave(G, 1).transpose(0, 1) for t in (k, v))  # [H, n, d]
+        qb = q[b].double().transpose(0, 1)
+        x = qb @ kb.transpose(1, 2) / math.sqrt(d)
+        A = float((qb.abs() @ kb.abs().transpose(1, 2)).max()) / math.sqrt(d) if n else 0.0
+        if softcap:
+            x = softcap * torch.tanh(x / softcap)
+        at = torch.arange(Sq, device=DEV)[:, None] + n - Sq
+        j = torch.arange(n, device=DEV)
+        far = 0.0
+        if slopes is not None:
+            x = x - slopes.double()[:, None, None] * (at - j).abs()
+            far = float(slopes.max()) * (n + Sq)
+        ok = torch.ones(Sq, n, dtype=torch.bool, device=DEV)
+        right = 0 if causal else window[1]
+        if right >= 0:
+            ok &= j <= at + right
+        if window[0] >= 0:
+            ok &= j >= at - window[0]
+        x = x.masked_fill(~ok, -math.inf)
+        none = ~ok.any(1)
+        rl = torch.logsumexp(x, -1) if n else torch.full((H, Sq), -math.inf, device=DEV, dtype=torch.float64)
+        w = torch.exp(x - torch.where(none, 0.0, rl)[..., None])
+        ro, size = w @ vb, w @ vb.abs()
+        ds = 2.0 ** -17 * (1 + 2.0 ** -4) * A + softcap * 2.0 ** -20 + 2.0 ** -21 * far
+        got = lse[b].double()
+        assert torch.equal(got == -math.inf, none.expand(H, Sq))
+        err = torch.where(none, 0.0, (got - rl).abs())
+        assert bool((err <= ds + 2.0 ** -20 * (1 + torch.where(none, 0.0, rl.abs()))).all()), float(err.max())
+        err = (out[b].double().transpose(0, 1) - ro).abs()
+        bound = (pr + 2 * ds + 2.0 ** -18) * size + u * ro.abs() + 2.0 ** -25
+        assert bool((err <= bound).all()), (b, float((err / bound).max()))
+
+
+def queries(B, Sq, H, d, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(B, Sq, H, d, generator=g, device=DEV).to(dtype)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 66, 77, 259, 4001])
+def test_scales_word_by_word(fmt, d, n):
+    """Slabs of an odd number of rows (4001 aside, of a few tiles): the scales do not start on 16
+    bytes, so that every lane brings and announces its own.  Many warps begin at once."""
+    B = 40 if n < 1000 else 3
+    c = contiguous_cache(B, n, 3, d, fmt, seed=n)
+    q = queries(B, 2, 6, d, torch.bfloat16, n + 1)
+    out, lse = fa().fa_fwd_kvcache_quant(q, *c, causal=True)
+    check(out, lse, q, *values(c), [n] * B, causal=True)
+    for _ in range(20):
+        again = fa().fa_fwd_kvcache_quant(q, *c, causal=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
