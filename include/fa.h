@@ -484,10 +484,12 @@ FA_API int fa_kvcache_read_quant(const void *k_cache, const void *v_cache, const
  *   q, out [batch, seqlen_q, num_heads, head_dim] contiguous, 16-bit (dtype); lse, masks,
  *   softcap, ALiBi, cache_seqlens and block_table as for fa_fwd_kvcache; the cache, its scales
  *   and strides as for fa_kvcache_append_quant.
- * Scores, softmax and the sums are fp32; the probabilities are rounded to fp16 (relative
- *   2^-11; for fp16 outputs two parts, 2^-22) for their product with the values.  The keys are shared out evenly over the SMs,
- *   whatever the sequences' lengths, and a second launch joins the parts: the result depends
- *   on the share's borders within rounding only, and is the same for the same call.
+ * Scores, softmax and the sums are fp32.  For their product with the values' codes, each
+ *   probability times its value's scale is rounded to fp16: relative 2^-11 (for fp16 outputs two
+ *   parts, 2^-22), or 2^-38 of the largest such product that the query row has met where that is
+ *   more.  The keys are shared out evenly over the SMs, whatever the sequences' lengths, and a
+ *   second launch joins the parts: the result depends on the share's borders within rounding
+ *   only, and is the same for the same call.
  * Limits: batch <= 65535, seqlen_q <= 2^20, and batch * num_heads_k * (query rows / 16) *
  *   (capacity / 64) below 2^31.
  * Any number of query rows works; a KV head's cache is read once per 16 rows ((num_heads /

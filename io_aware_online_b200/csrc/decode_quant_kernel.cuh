@@ -34,11 +34,14 @@
 //   P V: O^T[16 head-dim x 8 rows] = V^T[16 x 16 keys] P^T[16 x 8].  A lane reads 16
 //     head-dim codes of four keys and pairs the bytes of two keys with a byte permute, which
 //     transposes them; P^T comes from the score layout by an 8 x 8 transpose in registers.
-//   P carries v's scale, relative to the largest scale that the warp has met, so that it fits
-//     fp16: p vscale / ref * 2^14 (full precision down to 2^-28 of the largest); O is rescaled
-//     when ref grows, as it is when the running max grows.  Rounding P to fp16 (2^-11 relative)
-//     is an eighth of a bf16 output's own rounding but as much as an fp16 output's: for those the
-//     remainder is a second operand on the same V registers (2^-22), half as many products more.
+//   P carries v's scale, so that it fits fp16 relative to the largest p vscale that its query row
+//     has met: p vscale / ref * 2^14, ref a power of two above that product (full precision down to
+//     2^-28 of the largest, steps of 2^-38 of it below).  O is rescaled when a product reaches ref, as
+//     it is when the running max grows.  (Relative to the largest vscale alone, a key of a large
+//     scale that weighs nothing, or that only another row sees, took the others' precision.)
+//     Rounding P to fp16 (2^-11 relative) is an eighth of a bf16 output's own rounding but as much
+//     as an fp16 output's: for those the remainder is a second operand on the same V registers
+//     (2^-22), half as many products more.
 //
 // Measured (B=64, 1K..32K keys, 8 KV heads, of the copy rate, rows of a head stored together):
 // d=128, 4 query heads per KV head, E4M3 385 .. 420 us (91-98%; the SM clock gives way at the power
@@ -285,12 +288,12 @@ struct DqRows {
 };
 
 // Products -> base-2 scores of a tile: scale, softcap, ALiBi and (unless every row sees all
-// of the tile) the mask; their max per row, and the largest value scale.
+// of the tile) the mask; their max per row, and the value scales.
 template <bool WHOLE, bool EXTRA, int NT>
 __device__ __forceinline__ void dq_scores(const DecodeQuantParams& p, const DqRows<NT>& rows,
                                           const DqSeq& sq, int key0, int perm, const float* sks,
                                           const float* svs, float2 (&x)[4][NT][2], float (&vs)[4][2],
-                                          float (&mx)[NT][2], float& vmax) {
+                                          float (&mx)[NT][2]) {
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -299,7 +302,6 @@ __device__ __forceinline__ void dq_scores(const DecodeQuantParams& p, const DqRo
       const float ks = sks[r];
       const bool in = WHOLE || (key >= sq.key_lo && key < sq.key_hi);
       vs[mt][h2] = in ? svs[r] : 0.f;
-      vmax = fmaxf(vmax, vs[mt][h2]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = mul2(make_float2(ks, ks), make_float2(rows.rf[nt][0], rows.rf[nt][1]));
@@ -327,30 +329,65 @@ __device__ __forceinline__ void dq_scores(const DecodeQuantParams& p, const DqRo
     }
 }
 
-// Scores -> probabilities, their sums, and P V over the tile.  SPLIT: what rounding P to fp16
-// leaves is a second operand, so that P carries 22 bits.
+// Scores -> probabilities times their values' scales; the probabilities' sums, and the largest
+// product of each row.
+template <bool WHOLE, int NT>
+__device__ __forceinline__ void dq_weights(float2 (&x)[4][NT][2], const float (&vs)[4][2],
+                                           const float2 (&m_neg)[NT], float2 (&l_run)[NT], float (&wm)[NT][2]) {
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        const float2 v = x[mt][nt][h2];
+        const float2 d = add2(v, m_neg[nt]);
+        const float2 pr = make_float2(ex2(d.x), ex2(d.y));
+        l_run[nt] = add2(l_run[nt], pr);
+        float2 w = mul2(pr, both(vs[mt][h2]));
+        if (!WHOLE) {  // a masked key's scale may be anything
+          w.x = v.x == -INFINITY ? 0.f : w.x;
+          w.y = v.y == -INFINITY ? 0.f : w.y;
+        }
+        x[mt][nt][h2] = w;
+      }
+      wm[nt][0] = max3f(wm[nt][0], x[mt][nt][0].x, x[mt][nt][1].x);
+      wm[nt][1] = max3f(wm[nt][1], x[mt][nt][0].y, x[mt][nt][1].y);
+    }
+}
+
+__device__ __forceinline__ float dq_pow2(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
+
+// The reference of a row's products is the power of two above the largest of them, `top`, kept as
+// inv = 2^14 / ref.  (At least 2^-112, so that inv and its inverse are normal numbers.)
+constexpr int kDqInvMax = 268 - 15;  // exponent field of inv for the smallest reference
+
+// Multiplies O by al and moves it from the reference behind inv to that of `top`.
+template <int KS>
+__device__ __forceinline__ void dq_rebase(float top, float al, int h, float& inv, float (&acc)[KS][4]) {
+  const int now = 268 - static_cast<int>(min(max((__float_as_uint(top) >> 23) + 1u, 15u), 253u));
+  // (beyond 2^127 only where al is 0, below 2^-126 only where nothing of O is left)
+  const int field = 127 + now - static_cast<int>(__float_as_uint(inv) >> 23);
+  const float f = al * dq_pow2(min(max(field, 0), 254));
+  inv = dq_pow2(now);
+#pragma unroll
+  for (int k = 0; k < KS; ++k) acc[k][h] *= f, acc[k][2 + h] *= f;
+}
+
+// P V over the tile, from the products of probabilities and scales.  SPLIT: what rounding them to
+// fp16 leaves is a second operand, so that they carry 22 bits.
 template <int D, bool E4M3, int NT, bool SPLIT, bool WHOLE>
 __device__ __forceinline__ void dq_values(const DqSeq& sq, int key0, const uint8_t* sV, int t4, int vchunk,
-                                          const float2 (&x)[4][NT][2], const float (&vs)[4][2], float inv,
-                                          const float2 (&m_neg)[NT], float2 (&l_run)[NT],
+                                          const float2 (&w)[4][NT][2], const float2 (&inv)[NT],
                                           float (&acc)[NT][D / 16][4]) {
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
     uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
     for (int h2 = 0; h2 < 2; ++h2) {
-      const float vf = vs[mt][h2] * inv;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float2 v = x[mt][nt][h2];
-        const float2 d = add2(v, m_neg[nt]);
-        const float2 pr = make_float2(ex2(d.x), ex2(d.y));
-        l_run[nt] = add2(l_run[nt], pr);
-        float2 pv = mul2(pr, make_float2(vf, vf));
-        if (!WHOLE) {  // a masked key's scale may be anything
-          pv.x = v.x == -INFINITY ? 0.f : pv.x;
-          pv.y = v.y == -INFINITY ? 0.f : pv.y;
-        }
+        const float2 pv = mul2(w[mt][nt][h2], inv[nt]);
         const uint32_t hi = pack2<false>(pv.x, pv.y);
         pb[nt][h2] = transpose8(hi);
         if constexpr (SPLIT) {
@@ -400,8 +437,8 @@ __device__ __forceinline__ void dq_values(const DqSeq& sq, int key0, const uint8
 // rows or as partial ones.
 template <int D, int NT, bool BF16>
 __device__ __forceinline__ void dq_write(const DecodeQuantParams& p, const DqWalk& wk, bool direct,
-                                         int64_t slot, int g, int t4, int vchunk, float unit,
-                                         const float (&m_run)[NT][2], const float2 (&l_run)[NT],
+                                         int64_t slot, int g, int t4, int vchunk, float per_inv,
+                                         const float2 (&inv)[NT], const float (&m_run)[NT][2], const float2 (&l_run)[NT],
                                          const float (&acc)[NT][D / 16][4]) {
   constexpr float kLn2 = 0.6931471805599453f;
 #pragma unroll
@@ -413,7 +450,7 @@ __device__ __forceinline__ void dq_write(const DecodeQuantParams& p, const DqWal
       for (int o = 4; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
       const int rr = nt * 8 + 2 * t4 + h, r = wk.grp * 8 * NT + rr;
       if (r >= p.R) continue;
-      const float m = m_run[nt][h];
+      const float m = m_run[nt][h], unit = per_inv / (h == 0 ? inv[nt].x : inv[nt].y);
       if (direct) {
         // no allowed key: l is 0 and the row is 0 with LSE -inf; a NaN stays one
         const float f = l == 0.f ? 0.f : unit / l;
@@ -453,7 +490,7 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
                         const __grid_constant__ CUtensorMap tmV, const DecodeQuantParams p) {
   using Cfg = DqCfg<D, NT>;
   constexpr float kLog2e = 1.4426950408889634f;
-  constexpr float kUnit = (E4M3 ? 256.f : 1.f) / 16384.f;  // acc * ref * kUnit is in units of v
+  constexpr float kUnit = E4M3 ? 256.f : 1.f;  // acc * kUnit / inv is in units of v
   constexpr int KS = D / 16;      // k-steps of the scores, and 16-row blocks of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -628,10 +665,13 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
 
     float m_run[NT][2], acc[NT][KS][4];
     float2 l_run[NT];
-    float ref = 0.f;  // power of two above every value scale met so far; 0: none yet
+    float top[NT][2];  // the largest product of a probability and a value scale met so far
+    float2 inv[NT];    // 2^14 by the power of two above it
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m_run[nt][0] = m_run[nt][1] = -INFINITY;
+      top[nt][0] = top[nt][1] = 0.f;
+      inv[nt] = both(dq_pow2(kDqInvMax));
       l_run[nt] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -707,17 +747,17 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
             x[mt][nt][0] = make_float2(c4[mt][nt][0], c4[mt][nt][1]);
             x[mt][nt][1] = make_float2(c4[mt][nt][2], c4[mt][nt][3]);
           }
-        // ---- base-2 scores, the tile's max per row and largest value scale
+        // ---- base-2 scores, the tile's max per row
         const int key0 = (sq.t_lo + wk.at + t) * kDqTok;
         const bool whole = key0 >= all_lo && key0 + kDqTok - 1 <= all_hi;
         float vs[4][2];  // value scales of this lane's keys
-        float mx[NT][2], vmax = 0.f;
+        float mx[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
         if (whole)
-          dq_scores<true, EXTRA, NT>(p, rows, sq, key0, perm, sks, svs, x, vs, mx, vmax);
+          dq_scores<true, EXTRA, NT>(p, rows, sq, key0, perm, sks, svs, x, vs, mx);
         else
-          dq_scores<false, EXTRA, NT>(p, rows, sq, key0, perm, sks, svs, x, vs, mx, vmax);
+          dq_scores<false, EXTRA, NT>(p, rows, sq, key0, perm, sks, svs, x, vs, mx);
         // the K tile and the scales are used: bring the next ones
         __syncwarp();
         if (follows) {
@@ -725,52 +765,60 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
           filled_k += fw.sq.key_hi > fw.sq.key_lo;
         }
 #pragma unroll
-        for (int o = 4; o < 32; o *= 2) {
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+        for (int o = 4; o < 32; o *= 2)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               mx[nt][h] = fmaxf(mx[nt][h], __shfl_xor_sync(0xffffffffu, mx[nt][h], o));
-        }
-        // ---- grown max or scale: O and the sums move to the new reference
-        bool grown = vmax > ref;
+        // ---- grown max: the sums, O and the products' reference move with it
+        bool grown = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) grown |= mx[nt][h] > m_run[nt][h];
         if (__any_sync(0xffffffffu, grown)) {
-          float fref = 1.f;
-          if (vmax > ref) {
-            // (at least 2^-112, so that 2^14 / ref and its inverse are normal numbers)
-            const uint32_t e = min(max((__float_as_uint(vmax) >> 23) + 1u, 15u), 253u);
-            const float nref = __uint_as_float(e << 23);
-            fref = ref * __uint_as_float((254u - e) << 23);  // ref / nref, a power of two (or 0)
-            ref = nref;
-          }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float al[2];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float m_new = fmaxf(m_run[nt][h], mx[nt][h]);
-              al[h] = m_new == -INFINITY ? 1.f : ex2(m_run[nt][h] - m_new);
+              const float al = m_new == -INFINITY ? 1.f : ex2(m_run[nt][h] - m_new);
               m_run[nt][h] = m_new;
+              (h == 0 ? l_run[nt].x : l_run[nt].y) *= al;
+              top[nt][h] *= al;
+              dq_rebase<KS>(top[nt][h], al, h, h == 0 ? inv[nt].x : inv[nt].y, acc[nt]);
             }
-            l_run[nt] = mul2(l_run[nt], make_float2(al[0], al[1]));
-#pragma unroll
-            for (int k2 = 0; k2 < KS; ++k2)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][k2][e] *= al[e & 1] * fref;
-          }
         }
         float2 m_neg[NT];  // minus the max (0 while a row has met no key)
+        float wm[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           m_neg[nt] = make_float2(m_run[nt][0] == -INFINITY ? 0.f : -m_run[nt][0],
                                   m_run[nt][1] == -INFINITY ? 0.f : -m_run[nt][1]);
-        // 2^14 / ref: exponent field 254 - e + 14, at most 253 (ref = 0 only while every scale was 0)
-        const float inv = ref > 0.f ? __uint_as_float((268u - (__float_as_uint(ref) >> 23)) << 23) : 0.f;
+          wm[nt][0] = wm[nt][1] = 0.f;
+        }
+        if (whole)
+          dq_weights<true, NT>(x, vs, m_neg, l_run, wm);
+        else
+          dq_weights<false, NT>(x, vs, m_neg, l_run, wm);
+        // ---- a product that reaches the reference: it moves above the tile's largest
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          over |= wm[nt][0] * inv[nt].x >= 16384.f || wm[nt][1] * inv[nt].y >= 16384.f;
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int o = 4; o < 32; o *= 2)
+                wm[nt][h] = fmaxf(wm[nt][h], __shfl_xor_sync(0xffffffffu, wm[nt][h], o));
+              top[nt][h] = fmaxf(top[nt][h], wm[nt][h]);
+              dq_rebase<KS>(top[nt][h], 1.f, h, h == 0 ? inv[nt].x : inv[nt].y, acc[nt]);
+            }
+        }
         ok = dq_wait(p, fullV, phase);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -778,9 +826,9 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
         }
         phase ^= 1;
         if (whole)
-          dq_values<D, E4M3, NT, !BF16, true>(sq, key0, bufV, t4, vchunk, x, vs, inv, m_neg, l_run, acc);
+          dq_values<D, E4M3, NT, !BF16, true>(sq, key0, bufV, t4, vchunk, x, inv, acc);
         else
-          dq_values<D, E4M3, NT, !BF16, false>(sq, key0, bufV, t4, vchunk, x, vs, inv, m_neg, l_run, acc);
+          dq_values<D, E4M3, NT, !BF16, false>(sq, key0, bufV, t4, vchunk, x, inv, acc);
         __syncwarp();
       } else if (follows) {  // no keys: nothing was brought, the buffers are free
         dq_fill<D, NT, false>(p, &tmK, fw, bufK, sks, fullK);
@@ -803,7 +851,7 @@ __global__ void __launch_bounds__(DqCfg<D, NT>::kThreads, 1)
     }
     const bool direct = wk.at == 0 && cnt == sq.n;  // the whole pair lies in this share
     const int64_t slot = 2 * static_cast<int64_t>(share_id) + (wk.n == 0 ? 0 : 1);
-    dq_write<D, NT, BF16>(p, wk, direct, slot, g, t4, vchunk, ref * kUnit, m_run, l_run, acc);
+    dq_write<D, NT, BF16>(p, wk, direct, slot, g, t4, vchunk, kUnit, inv, m_run, l_run, acc);
     // the warp that begins a pair notes which slots hold its pieces
     if (wk.at == 0 && lane == 0) {
       const int64_t pair = static_cast<int64_t>(wk.b) * pairs + wk.hk * p.groups + wk.grp;
