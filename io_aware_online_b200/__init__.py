@@ -595,7 +595,7 @@ def _int32(n) -> int:
 def _on(fn, args):
     """fn(**args) on args["stream"], another stream than the current one perhaps.  What the call
     allocates has to be that stream's (memory freed on the current stream may still be in use
-    there), and what it returns is freed for work of both."""
+    there); its arguments and what it returns are freed for work of both."""
     stream = args.pop("stream")
     first = next((t for t in args.values() if torch.is_tensor(t)), None)
     if first is None or not first.is_cuda:
@@ -609,6 +609,9 @@ def _on(fn, args):
     with torch.cuda.stream(stream):
         result = fn(**args)
     if handle != current.cuda_stream:
+        for t in args.values():
+            if torch.is_tensor(t):
+                t.record_stream(stream)
         for t in result if isinstance(result, tuple) else (result,):
             if t is not None:
                 t.record_stream(current)

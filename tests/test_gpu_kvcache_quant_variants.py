@@ -121,3 +121,25 @@ def test_scales_word_by_word(fmt, d, n):
     for _ in range(20):
         again = fa().fa_fwd_kvcache_quant(q, *c, causal=True)
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_temporaries_on_another_stream():
+    """Arguments that the caller drops right after a call on another stream: their memory is not given
+    to the current stream's work while the call still waits to read them."""
+    lens = [700, 90]
+    c = contiguous_cache(2, 700, 2, 64, "e4m3", True, seed=5)
+    q = queries(2, 1, 4, 64, torch.float16, 6)
+    cs = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ref = fa().fa_fwd_kvcache_quant(q, *c, cache_seqlens=cs)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        tmp = q.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = fa().fa_fwd_kvcache_quant(tmp, *c, cache_seqlens=cs, stream=stream)
+        del tmp
+        torch.empty_like(q).fill_(3)  # takes a freed block of that size
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
