@@ -384,8 +384,9 @@ FA_API int fa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_ou
  * q, k are the forward's inputs; the other arguments must be those of the forward call.
  * All six row tensors take strides as there; dq may be dq_out and dk dk_out (same pointer and
  * strides).  Without the norm dx is g.  r is computed again from x, so the forward saves nothing.
- * workspace: >= fa_qk_norm_rope_bwd_workspace_size(batch, seqlen, head_dim) bytes, 16-byte
- * aligned, needed when a weight gradient is asked for; calls sharing it must be stream-ordered.
+ * workspace: >= fa_qk_norm_rope_bwd_workspace_size(batch, seqlen, head_dim) bytes (asked with the
+ * call's device current), 16-byte aligned, needed when a weight gradient is asked for; calls sharing
+ * it must be stream-ordered.
  * Deterministic: the order of the sums depends on the sizes and the device's SM count only.
  */
 FA_API size_t fa_qk_norm_rope_bwd_workspace_size(int batch, int seqlen, int head_dim);
@@ -495,8 +496,9 @@ FA_API int fa_kvcache_read_quant(const void *k_cache, const void *v_cache, const
  * Any number of query rows works; a KV head's cache is read once per 16 rows ((num_heads /
  *   num_heads_k) * seqlen_q), so long prompts are better read back (fa_kvcache_read_quant)
  *   and attended with fa_fwd.
- * workspace: >= fa_kvcache_quant_workspace_size(...) bytes, 16-byte aligned, required; it
- *   needs no initialisation, and calls sharing it must be stream-ordered.
+ * workspace: >= fa_kvcache_quant_workspace_size(...) bytes (asked with the call's device current),
+ *   16-byte aligned, required; it needs no initialisation, and calls sharing it must be
+ *   stream-ordered.
  * Rows of the cache at or past cache_seqlens[b], and blocks past a sequence's last page, may
  *   hold anything.
  */

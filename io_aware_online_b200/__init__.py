@@ -573,6 +573,14 @@ def _is_packed(name, t, cu_seqlens_new):
                          "with cu_seqlens_new")
 
 
+def _size(fn, dev, *args) -> int:
+    """The bytes fn(*args) that a call on the tensors' device needs (they go by its SMs)."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _launch(fn, dev, *args):
     """Calls fn(*args, stream) for the current stream of the tensors' device, with that device
     current (the C ABI launches there)."""
@@ -722,7 +730,7 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, *, q_weight=None, k_weight=None, e
     dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     args = _rope_args(d, dtype, dev, q_weight, k_weight, eps, norm, cos, sin, interleaved)
-    workspace = _workspace(workspace, lib.fa_qk_norm_rope_bwd_workspace_size(B, S, d), q.device, dev)
+    workspace = _workspace(workspace, _size(lib.fa_qk_norm_rope_bwd_workspace_size, dev, B, S, d), q.device, dev)
     _launch(lib.fa_qk_norm_rope_bwd, dev, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
             k.data_ptr(), dq.data_ptr(), dk.data_ptr(), 0 if dwq is None else dwq.data_ptr(),
             0 if dwk is None else dwk.data_ptr(), dt, B, S, H, ks[2], d, *strides, sq, sk, sdq, sdk,
@@ -884,7 +892,7 @@ def fa_fwd_kvcache_quant(q, k_cache, v_cache, k_scale, v_scale, *, cache_seqlens
         out = _like(q)
     if lse is None and return_lse:
         lse = q.new_empty((B, H, sq), dtype=torch.float32)
-    workspace = _workspace(workspace, lib.fa_kvcache_quant_workspace_size(B, sq, H, Hkv, d), q.device, dev)
+    workspace = _workspace(workspace, _size(lib.fa_kvcache_quant_workspace_size, dev, B, sq, H, Hkv, d), q.device, dev)
     _launch(lib.fa_fwd_kvcache_quant, dev, q.data_ptr(), *ptrs, _want("out", out, shape, dtype, dev),
             _want("lse", lse, (B, H, sq), torch.float32, dev), dt, fmt, B, sq, H, Hkv, d, cst, *paging,
             _want("cache_seqlens", cache_seqlens, (B,), torch.int32, dev),

@@ -124,3 +124,13 @@ def test_the_current_stream_needs_no_marks(gpu, i):
         fn, args, kw = entry_points()[i]
         fn(*args, **kw, **kw_stream)
         assert not any("seen" in t.__dict__ for t in [*args, *kw.values()] if torch.is_tensor(t))
+
+
+@pytest.mark.parametrize("i", range(len(IDS)), ids=IDS)
+def test_the_library_is_asked_on_the_tensors_device(gpu, i):
+    """Sizes of workspaces depend on the current device's SMs, as the grid does."""
+    fn, args, kw = entry_points()[i]
+    fn(*args, **kw)
+    assert fn.__name__ in [c[0] for c in gpu.lib.calls]
+    assert {c[1] for c in gpu.lib.calls} == {1}
+    assert gpu.device == 0
