@@ -364,8 +364,9 @@ FA_API int fa_bwd(const void *dout, const void *q, const void *k, const void *v,
  *   rotary_dim: a multiple of 16 up to head_dim.  Both NULL leaves the rotation out.
  * positions: int32 [batch, seqlen] contiguous, or NULL (position = index along seqlen).  A
  *   position outside [0, max_positions) uses the nearest row and raises FA_DEV_BAD_POSITION.
- * Arithmetic in fp32, rounded once to dtype.  A row whose sum of squares leaves fp32's range
- * (elements above about 1e18, possible in bf16 only) is not supported.
+ * Arithmetic in fp32, rounded once to dtype.  A row whose sum of squares leaves fp32's range is
+ * not supported (possible in bf16 only: elements above about 1e18, and with eps = 0 rows of
+ * elements below about 1e-19).  With eps = 0 a row of zeros gives NaN, as the formula does.
  */
 FA_API int fa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int dtype,
                            int batch, int seqlen, int num_heads, int num_heads_k, int head_dim,
@@ -418,7 +419,10 @@ FA_API int fa_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const voi
  * Quantising.  For a row with largest magnitude m: scale = m / top (top = 448 for E4M3, 127
  *   for integers), code = x * top / m rounded correctly to the format (ties to even).  A row of
  *   zeros gets scale 0; one with an infinity or a NaN reads back as NaN throughout.  Codes
- *   with the bits of an E4M3 NaN are never written, and must not lie in an attended range.
+ *   with the bits of an E4M3 NaN are never written.  Whoever fills a cache otherwise has to keep
+ *   them out of attended ranges, and scales at 0 or above: in a key such a code makes the scores
+ *   NaN and it reads back as NaN, but in a value the attention takes it for 480 (looking for
+ *   them would cost it 3 to 10%).
  * k_new, v_new: [batch, seqlen_new, num_heads_k, head_dim] with element strides k_strides,
  *   v_strides (as fa_qk_norm_rope); or packed, with cu_seqlens_new (device int32 [batch + 1],
  *   nondecreasing from 0): [seqlen_new, num_heads_k, head_dim], seqlen_new then being the
@@ -465,9 +469,10 @@ FA_API int fa_qk_norm_rope_append_quant(const void *q, const void *k, const void
  * fa_kvcache_read_quant -- reads rows of an 8-bit cache back into packed 16-bit tensors (for
  * a chunked prefill: fa_fwd's varlen form attends them).
  *   k_out, v_out [total, num_heads_k, head_dim] contiguous; row cu_seqlens[b] + t gets
- *   position seq_start[b] + t (seq_start int32 [batch], NULL = zeros) of sequence b, rounded
- *   once to dtype.  cu_seqlens: device int32 [batch + 1], nondecreasing from 0; rows from
- *   cu_seqlens[batch] on are left as they were.
+ *   position seq_start[b] + t (seq_start int32 [batch], NULL = zeros) of sequence b: code * scale
+ *   rounded to fp32, then that to dtype (together at most 2^-24 beyond half a step of dtype).
+ *   cu_seqlens: device int32 [batch + 1], nondecreasing from 0; rows from cu_seqlens[batch] on
+ *   are left as they were.
  * Positions and blocks outside the cache read as zeros and raise FA_DEV_BAD_LENGTH /
  * FA_DEV_BAD_BLOCK.
  */

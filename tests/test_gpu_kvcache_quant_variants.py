@@ -143,3 +143,25 @@ def test_temporaries_on_another_stream():
         torch.empty_like(q).fill_(3)  # takes a freed block of that size
         torch.cuda.synchronize()
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_read_back_rounds_to_fp32_first(fmt, dtype):
+    """Bit for bit the product in fp32, rounded to 16 bits; over enough rows that some differ from the
+    exact product rounded once."""
+    n, Hkv, d = 20000, 4, 64
+    c = contiguous_cache(1, n, Hkv, d, fmt, seed=9)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    got = fa().fa_kvcache_read_quant(*c, cu, total=n, dtype=dtype)
+    once = 0
+    for out, code, scale in zip(got, c[:2], c[2:]):
+        s = scale[0].t()[..., None]
+        assert torch.equal(out, (code[0].float() * s).to(dtype))
+        exact = code[0].double() * s.double()
+        err = (out.double() - exact).abs()
+        half = torch.finfo(dtype).eps / 2 + 2.0 ** -24
+        assert bool((err <= half * exact.abs() + 2.0 ** -25).all())
+        # (a double rounds to 16 bits by way of fp32 too, so a wrong rounding shows as an error above half)
+        once += int((err > torch.finfo(dtype).eps / 2 * 2.0 ** torch.floor(torch.log2(exact.abs().clamp(min=1e-30)))).sum())
+    assert once > 0
