@@ -165,3 +165,45 @@ def test_read_back_rounds_to_fp32_first(fmt, dtype):
         # (a double rounds to 16 bits by way of fp32 too, so a wrong rounding shows as an error above half)
         once += int((err > torch.finfo(dtype).eps / 2 * 2.0 ** torch.floor(torch.log2(exact.abs().clamp(min=1e-30)))).sum())
     assert once > 0
+
+
+LENS = [700, 130, 2048, 5, 1, 0, 333]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Sq,H,Hkv", [(1, 8, 2), (2, 16, 2), (3, 6, 2), (11, 3, 3), (6, 18, 3)])
+@pytest.mark.parametrize("terms", ["none", "softcap", "alibi", "both"])
+def test_every_variant(fmt, d, dtype, Sq, H, Hkv, terms):
+    """Both formats, head dims and types, up to 8, 16 and 36 query rows per KV head, with and without the
+    terms that need code of their own."""
+    c = contiguous_cache(len(LENS), 2048, Hkv, d, fmt, d == 64, seed=Sq + d)
+    q = queries(len(LENS), Sq, H, d, dtype, H)
+    kw = dict(causal=Sq != 3)
+    if terms in ("softcap", "both"):
+        kw["softcap"] = 12.0
+    slopes = 2.0 ** -torch.arange(1, H + 1, device=DEV).float() if terms in ("alibi", "both") else None
+    if terms == "both":
+        kw["window"] = (500, 2)
+    call = {("window_size" if k == "window" else k): v for k, v in kw.items()}
+    cs = torch.tensor(LENS, dtype=torch.int32, device=DEV)
+    out, lse = fa().fa_fwd_kvcache_quant(q, *c, cache_seqlens=cs, alibi_slopes=slopes, **call)
+    check(out, lse, q, *values(c), LENS, slopes=slopes, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Sq,H,Hkv", [(1, 8, 8), (2, 16, 2), (5, 8, 2)])
+def test_long_shares(fmt, d, dtype, Sq, H, Hkv):
+    """Many tiles a warp, so that its buffers are refilled often, and shares that end inside most pairs."""
+    lens = [9000, 20001, 64, 15000, 7777, 1, 12000]
+    c = contiguous_cache(len(lens), 20001 + 3, Hkv, d, fmt, True, seed=d)
+    q = queries(len(lens), Sq, H, d, dtype, 3)
+    cs = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out, lse = fa().fa_fwd_kvcache_quant(q, *c, cache_seqlens=cs, causal=True)
+    check(out, lse, q, *values(c), lens, causal=True)
+    for _ in range(5):
+        again = fa().fa_fwd_kvcache_quant(q, *c, cache_seqlens=cs, causal=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)

@@ -113,3 +113,26 @@ def run(B, S, H, Hkv, d, dtype, rot, inter, eps, seed):
 def test_no_eps(dtype, d, H, Hkv):
     """eps = 0 with rows that are not zero; the last group of a token's heads is partly empty."""
     run(2, 45, H, Hkv, d, dtype, d // 2, False, 0.0, seed=d + H)
+
+
+@pytest.mark.parametrize("B,S,H,Hkv,d,dtype,rot,inter", [
+    (2, 6001, 32, 8, 128, torch.bfloat16, 128, False),   # 51 groups a warp: a training batch
+    (1, 9000, 33, 9, 64, torch.float16, 32, True),       # 27, heads that do not fill a group
+    (1, 50001, 4, 4, 128, torch.float16, 64, False),     # one group a token, 43 tokens a warp
+    (1, 50001, 3, 8, 64, torch.bfloat16, 64, True),
+    (700, 90, 8, 1, 64, torch.bfloat16, 0, False),       # 54, many short sequences, no rotation
+])
+def test_many_groups_per_warp(B, S, H, Hkv, d, dtype, rot, inter):
+    """Each warp's slots of the copy ring are filled many times over, and positions looked up more than
+    once; also with the gradients written where the outputs' gradients were."""
+    assert rows_per_lane(B * S, H, Hkv, d) >= 8
+    (gq, gk, q, k, call), got = run(B, S, H, Hkv, d, dtype, rot, inter, 1e-6, seed=S)
+    again = fa().fa_qk_norm_rope_bwd(gq, gk, q, k, **call)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+    for _ in range(3):
+        a, b = gq.clone(), gk.clone()
+        inplace = fa().fa_qk_norm_rope_bwd(a, b, q, k, dq=a, dk=b, **call)
+        assert inplace[0] is a and inplace[1] is b
+        for x, y in zip(inplace, got):
+            assert torch.equal(x, y)
