@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(kBwdThreads, kRowsBwdBlocksPerSm)
   }
 }
 
-// dw[t][col] = sum over the blocks of ws[block][t][col].  A warp per column group of 32:
-// block y of 8 warps takes every eighth partial, then one sum over the warps.
+// dw[t][col] = sum over the blocks of ws[block][t][col].  A block per 32 columns: each of its 32
+// warps takes every 32nd partial, then the first adds up the warps' sums.
 constexpr int kDwWarps = 32;
 
 __global__ void __launch_bounds__(kDwWarps * 32) rows_bwd_dw_kernel(const RowsBwdParams p, int D) {
