@@ -497,20 +497,24 @@ def fa_bwd(dout, q, k, v, out, lse, *, cu_seqlens_q=None, cu_seqlens_k=None,
 # ------------------------------------------------------------------ arguments of the calls below
 # A decoding step calls these many times for a few microseconds of GPU work each, so the checks
 # read each property once and hand plain integers to ctypes.
-_STRIDES = {}  # (a, b, c) -> (address, int64[3] holding them)
-_STRIDES_BEFORE = {}  # the full table before it: calls that run now may still use its arrays
+_STRIDES = {}  # (a, b, c) -> the address of an int64[3] holding them
+
+
+class _Address(int):
+    """The address of an array, which lives as long as this number."""
 
 
 def _s3(a, b, c) -> int:
-    """Address of an int64[3] holding (a, b, c); equal triples share one."""
-    global _STRIDES, _STRIDES_BEFORE
-    e = _STRIDES.get((a, b, c))
-    if e is None:
+    """Address of an int64[3] holding (a, b, c), for as long as the caller keeps it; equal triples
+    share one."""
+    at = _STRIDES.get((a, b, c))
+    if at is None:
         if len(_STRIDES) >= 16384:
-            _STRIDES_BEFORE, _STRIDES = _STRIDES, {}
-        arr = (ctypes.c_int64 * 3)(a, b, c)
-        e = _STRIDES[(a, b, c)] = (ctypes.addressof(arr), arr)
-    return e[0]
+            _STRIDES.clear()
+        array = (ctypes.c_int64 * 3)(a, b, c)
+        at = _STRIDES[(a, b, c)] = _Address(ctypes.addressof(array))
+        at.array = array
+    return at
 
 
 def _like(t):

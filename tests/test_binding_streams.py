@@ -134,3 +134,14 @@ def test_the_library_is_asked_on_the_tensors_device(gpu, i):
     assert fn.__name__ in [c[0] for c in gpu.lib.calls]
     assert {c[1] for c in gpu.lib.calls} == {1}
     assert gpu.device == 0
+
+
+def test_strides_outlive_the_table_that_shares_them():
+    """A thread that has its strides and is put aside while others fill the table twice over."""
+    import ctypes
+    mine = [fa._s3(8 * i, 1 << 40, 24 + i) for i in range(50)]
+    for i in range(3 * 16384):
+        fa._s3(i, 7, 7)
+    for i, at in enumerate(mine):
+        assert list((ctypes.c_int64 * 3).from_address(int(at))) == [8 * i, 1 << 40, 24 + i]
+    assert len(fa._STRIDES) <= 16384
