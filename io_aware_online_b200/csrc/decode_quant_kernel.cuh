@@ -44,14 +44,17 @@
 //     (2^-22), half as many products more.  (For bf16 outputs too it would cost 0-8% at d=128, 7%
 //     at d=64 and 11-15% with 16 rows, for an error of 1.66e-3 in place of 1.67e-3.)
 //
-// Measured (B=64, 1K..32K keys, 8 KV heads, of the copy rate, rows of a head stored together):
-// d=128, 4 query heads per KV head, E4M3 385 .. 420 us (91-98%; the SM clock gives way at the power
-// limit), int8 385 us (99%, 436 us back to back for seconds); d=64 215 us (92%) and 233 us (85%):
-// there, and with 16 query rows (467 and 547 us, 82% and 70%), the issue of instructions and the
-// logic pipe (57-63% busy) bound it.  fp16 outputs, with the second part of P: d=128 392 us E4M3
-// and 416 us int8, d=64 229 and 252, 16 rows 535 and 600.  Rows of all heads together: 480 and 490 us at d=128, since a
-// tile is then 64 pieces of 128 bytes, 1 KB apart.  Few keys (8 x 1000): 12.8 us, all latency: the
-// share 2.5 us, the first tile's way 1.5, one tile's chain 3, the join 4.
+// Measured (B=64, 1K..32K keys, 8 KV heads, 4 query heads each, bf16, graph replays on several boxes,
+// of the copy rate; 2.32 GB at d=128: 353 us).  Rows of all heads together, the default order: d=128
+// E4M3 440-447 us (79-80%), int8 414-445 (79-85%), since a tile is then 64 pieces of 128 bytes, 1 KB
+// apart; d=64 240 (76%) and 220-240 (76-82%).  Rows of a head together: d=128 357-392 us (90-99%; 396
+// back to back for seconds, where the SM clock gives way at the power limit) and 367-384 (92-96%),
+// d=64 198-208 (88-92%) and 220-224 (81-83%): there, and with 16 query rows (460-466 and 520-530 us,
+// 76% and 67%), the issue of instructions and the logic pipe (58-63% busy) bound it.  fp16 outputs,
+// with the second part of P: d=128 E4M3 351-362, d=64 int8 240-254, 16 rows int8 578-589.  More rows
+// read a cache again for every 16 (64 sequences of 1K..8K keys, E4M3: 16 rows 150 us, 32 276, 64 545;
+// the bytes alone 95).  Few keys (8 x 1000): 11.9 us, all latency: the share 2.5 us, the first
+// tile's way 1.5, one tile's chain 3, the join 4.
 #pragma once
 
 #include <climits>

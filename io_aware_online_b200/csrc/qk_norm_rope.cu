@@ -460,8 +460,8 @@ cudaError_t launch_rows_inst(RowsParams p, cudaStream_t stream) {
 // both).  A lane sums dw over its rows in registers, a block over its warps in shared memory,
 // and a second small launch over the blocks.  The order of the sums depends on the sizes and
 // the SM count alone, so the same call gives the same bits.
-//   (Measured, 2 x 6001 tokens of 32 + 8 heads, d=128, bf16: 72 us with the second launch, 80% of
-//   the copy rate; without the ring, two groups per warp in registers, 97 us.  Several waves, each
+//   (Measured, 2 x 6001 tokens of 32 + 8 heads, d=128, bf16: 69-72 us with the second launch, 80-82%
+//   of the copy rate (a call 76 us); without the ring, two groups per warp in registers, 97 us.  Several waves, each
 //   block with its own partial sums, are slower.  59% of the issue slots; the second launch brought
 //   to the SMs early, as the attention's join is, gains nothing: the registers are all taken.)
 constexpr int kBwdThreads = 256;
